@@ -317,7 +317,9 @@ struct PolicyRows {
 // l = max(-A r, -A clip(r, 1 - low, 1 + high)), r = exp(logp - old), bounded by
 // -A dual_clip for A < 0 when dual_clip > 0; + kl_coef (e^t - t - 1) with
 // t = ref - logp; - entropy_coef ent; times the row's weight.  g = dl/dlogp,
-// h = dl/dent.  A zero advantage has no surrogate, whatever the ratio.
+// h = dl/dent.  A zero advantage has no surrogate, whatever the ratio.  A NaN ratio stays
+// NaN in l and g (the clip alone would make a number of it), and so does a NaN logp where
+// the surrogate does not depend on it.
 struct PolicyIn {
   float advantage, old_logp, ref_logp, weight;
 };
@@ -334,13 +336,14 @@ __device__ __forceinline__ float policy_row(const PolicyRows& q, const PolicyIn&
     const float r = q.old_logp != nullptr ? expf(logp - in.old_logp) : 1.f;
     const float u = -A * r;
     const float c = -A * fminf(fmaxf(r, 1.f - q.clip_low), 1.f + q.clip_high);
-    l = u >= c ? u : c;
-    dl = u >= c ? u : 0.f;  // d(-A r)/dlogp = -A r
+    l = u < c ? c : u;
+    dl = u < c ? 0.f : u;  // d(-A r)/dlogp = -A r
     if (A < 0.f && q.dual_clip > 0.f && l > -A * q.dual_clip) {
       l = -A * q.dual_clip;
       dl = 0.f;
     }
   }
+  if (isnan(logp)) l = dl = logp;
   if (q.kl_coef != 0.f) {
     const float t = in.ref_logp - logp, em1 = expm1f(t);
     l += q.kl_coef * (em1 - t);

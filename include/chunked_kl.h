@@ -371,7 +371,8 @@ int kl_logp_bwd(const kl_logp_problem* p, void* ws, size_t ws_bytes, const float
  *         + kl_coef (e^t - t - 1) - entropy_coef ent,
  *   loss = (1 / n) sum_n row_weight_n l_n,  n = normalizer if > 0, else the number
  * of rows that take part.  Where the two terms of the maximum are equal the
- * unclipped one gives the gradient. */
+ * unclipped one gives the gradient.  A NaN log-probability, or a NaN that the terms
+ * above depend on, makes the row's loss, the loss and the gradients NaN. */
 typedef struct kl_policy {
   const float* advantage;  /* [N]                                                 */
   const float* old_logp;   /* [N] of the policy that sampled; NULL: r = 1 (and its
