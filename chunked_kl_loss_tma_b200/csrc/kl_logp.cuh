@@ -711,8 +711,8 @@ __device__ __forceinline__ double pair_loss(const PrefPairs& q, const double* sc
   }
   const double y = beta * x - q.margin;
   if (q.loss == 2) {
-    *slope = y < 1.0 ? -beta : 0.0;
-    return y < 1.0 ? 1.0 - y : 0.0;
+    *slope = y >= 1.0 ? 0.0 : y < 1.0 ? -beta : y;  // a NaN margin is no satisfied one
+    return y >= 1.0 ? 0.0 : 1.0 - y;
   }
   // (1 - eps) softplus(-y) + eps softplus(y); d/dy = sigmoid(y) - (1 - eps)
   const double t = exp(-fabs(y)), soft = log1p(t), eps = q.smoothing;

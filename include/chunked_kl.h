@@ -411,7 +411,8 @@ int kl_policy_fwd_bwd(const kl_logp_problem* p, const kl_policy* q, void* ws, si
  * loss = the pairs' sum / (normalizer if > 0, else n_pairs).  A sequence may be in
  * any number of pairs (explicit pairs cost time in n_seqs x n_pairs, 4 ms at 65536
  * each).  A pair that names a sequence outside [0, n_seqs) sets KL_ERR_INDEX and
- * counts as 0. */
+ * counts as 0.  A NaN score or reference makes the loss and the gradients of its pairs'
+ * sequences NaN. */
 #define KL_PREFERENCE_SIGMOID 0
 #define KL_PREFERENCE_SQUARED 1
 #define KL_PREFERENCE_HINGE 2

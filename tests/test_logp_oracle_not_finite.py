@@ -30,3 +30,15 @@ def test_policy(where, sign, kw):
     assert np.isnan(o["loss"])
     for x in (o["row_loss"], o["g"]):
         assert np.flatnonzero(np.isnan(x)).tolist() == [ROW]
+
+
+@pytest.mark.parametrize("where", ["H", "ref_logp"])
+@pytest.mark.parametrize("kw", [dict(), dict(loss="squared"), dict(loss="hinge"),
+                                dict(loss="hinge", margin=0.2, average=True)])
+def test_preference(where, kw):
+    cu, ref = np.array([0, 2, 6, 7, 9]), np.zeros(4)
+    if where == "ref_logp":
+        ref[1] = np.nan
+    o = lo.preference(_rows(where == "H", cu), cu, None, ref, **kw)
+    assert np.isnan(o["loss"]) and np.isnan(o["pair_loss"]).tolist() == [False, True]
+    assert np.flatnonzero(np.isnan(o["g"])).tolist() == [2, 3, 4, 5, 7, 8]

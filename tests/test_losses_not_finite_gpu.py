@@ -90,3 +90,40 @@ def test_infinite_ratios_are_clipped():
         out = ck.policy_fwd_bwd(H, W, ids, adv, old_logp=old, clip_high=0.25)
         assert out["row_loss"][ROW].item() == want and (out["dH"][ROW] == 0).all()
         assert out["loss"].isfinite() and out["dW"].isfinite().all()
+
+
+PREF = [dict(), dict(loss="squared"), dict(loss="hinge"), dict(loss="hinge", margin=0.3, beta=2.0),
+        dict(label_smoothing=0.1), dict(average=True)]
+
+
+@pytest.mark.parametrize("kw", PREF)
+@pytest.mark.parametrize("where", ["H", "ref_logp"])
+@pytest.mark.parametrize("more", [0, 1000])
+def test_preference(kw, where, more):
+    """A NaN in one sequence: its pair's loss and both its sequences' gradients; more:
+    rows beyond what one CTA scores."""
+    n = N + more
+    g = torch.Generator().manual_seed(3)
+    _, W, _ = _inputs(3)
+    H = torch.randn(n, D, generator=g).bfloat16().cuda()
+    ids = torch.randint(V, (n,), generator=g).cuda()
+    cu = torch.tensor([0, 30, 60, 90, n], dtype=torch.int32, device="cuda")
+    ref = torch.zeros(4, device="cuda")
+    clean = ck.preference_fwd_bwd(H, W, ids, cu, ref_logp=ref, **kw)
+    assert clean["loss"].isfinite()
+    H, ref = H.clone(), ref.clone()
+    if where == "H":
+        H[40] = NAN  # sequence 1, in pair (1, 3)
+    else:
+        ref[3] = NAN
+    out = ck.preference_fwd_bwd(H, W, ids, cu, ref_logp=ref, **kw)
+    assert out["loss"].isnan() and out["pair_loss"][1].isnan()
+    assert torch.equal(out["pair_loss"][0], clean["pair_loss"][0])
+    assert out["dH"][30:60].isnan().all() and out["dH"][90:].isnan().all()
+    for s in (slice(0, 30), slice(60, 90)):
+        assert torch.equal(out["dH"][s], clean["dH"][s])
+    assert out["dW"].isnan().all()
+    pairs = torch.tensor([[0, 2], [1, 3], [2, 0]], dtype=torch.int32, device="cuda")
+    f = ck.preference_fwd(H, W, ids, cu, pairs, ref_logp=ref, **kw)
+    assert f["loss"].isnan() and f["pair_loss"].isnan().tolist() == [False, True, False]
+    assert f["g_logp"].isnan().sum() == 30 + n - 90
