@@ -598,7 +598,8 @@ __global__ void __launch_bounds__(512) logp_dlogits_kernel(
     for (int k = 0; k < 8; ++k) {
       const float p = scale * f[k];
       const float lnp = (__log2f(f[k]) + off) * kLn2;
-      f[k] = v * 8 + k < V && p > 0.f ? -p * fmaf(rc.y, lnp + rc.z, rc.x) : 0.f;
+      // p ln p = 0 where p is 0; a NaN p stays NaN
+      f[k] = v * 8 + k < V && p != 0.f ? -p * fmaf(rc.y, lnp + rc.z, rc.x) : 0.f;
     }
     store8<__nv_bfloat16>(e + v * 8, f);
   }

@@ -127,3 +127,21 @@ def test_preference(kw, where, more):
     f = ck.preference_fwd(H, W, ids, cu, pairs, ref_logp=ref, **kw)
     assert f["loss"].isnan() and f["pair_loss"].isnan().tolist() == [False, True, False]
     assert f["g_logp"].isnan().sum() == 30 + n - 90
+
+
+@pytest.mark.parametrize("chunk", [0, 64])
+@pytest.mark.parametrize("kept", [True, False])
+def test_entropy_gradient(chunk, kept):
+    """With a gradient for the entropies, the row's probabilities are NaN in dW too, not
+    its own token's alone."""
+    H, W, ids = _inputs(4)
+    H[ROW, 3] = NAN
+    one = torch.ones(N, device="cuda")
+    kw = dict(chunk_tokens=chunk, keep_chunk=kept)
+    f = ck.logp_fwd(H, W, ids, want_entropy=True, **kw)
+    b = ck.logp_bwd(H, W, ids, f["lse"], one, g_entropy=one, entropy=f["entropy"],
+                    workspace=f["workspace"] if kept else None, **kw)
+    assert b["dH"][ROW].isnan().all() and b["dW"].isnan().all()
+    assert b["dH"].isnan().sum() == D
+    q = ck.policy_fwd_bwd(H, W, ids, one, entropy_coef=0.1, chunk_tokens=chunk)
+    assert q["dH"][ROW].isnan().all() and q["dW"].isnan().all()
