@@ -83,6 +83,19 @@ class _Call:
             self.head = (workspace.data_ptr(), _workspace(workspace, self.dev))
         self.ws = workspace
 
+    def rebind(self, H, W, ids, mask, T_row, cu_seqlens):
+        """The same problem with its tensors where they are now: saved tensors may have come
+        back at other addresses (a head that was freed and gathered again, hooks that keep
+        them on the host)."""
+        old = self.p
+        p, self.keep = make_logp_problem(
+            H, W, ids, T=old.T if T_row is None else T_row, mask=mask, cu_seqlens=cu_seqlens,
+            chunk_tokens=old.chunk_tokens, want_entropy=old.entropy, keep_chunk=old.keep_chunk,
+            dW_dtype=W.dtype)
+        if H.device != self.dev or (p.N, p.d, p.V, p.n_seqs) != (old.N, old.d, old.V, old.n_seqs):
+            raise ValueError("saved tensors of another shape or device than the forward's")
+        self.p = p
+
     def new(self, *shape):
         return torch.empty(shape, dtype=torch.float32, device=self.dev)
 
@@ -315,6 +328,7 @@ class _Fused(torch.autograd.Function):
         # ids, mask, T and cu_seqlens too: the backward reads them again
         ctx.save_for_backward(H, W, f["lse"], f.get("entropy"), f.get("g_logp"),
                               f.get("g_entropy"), *call.keep[2:6])
+        call.keep = None  # from here on autograd's saved tensors are what is held and read
         if ctx.scalar:
             return f["loss"]
         return (f["logp"], f["entropy"]) if f["entropy"] is not None else f["logp"]
@@ -322,8 +336,11 @@ class _Fused(torch.autograd.Function):
     @staticmethod
     def backward(ctx, g, g_ent=None):
         # refuses inputs that changed in place since the forward
-        H, W, lse, ent, g_logp, g_entropy = ctx.saved_tensors[:6]
+        H, W, lse, ent, g_logp, g_entropy, *rest = ctx.saved_tensors
         c, scale = ctx.call, g
+        c.rebind(H, W, *rest)
+        for t in (lse, ent, g_logp, g_entropy):
+            _rows(t, "a saved tensor", c.dev, c.N)
         if not ctx.scalar:
             scale = None
             g_logp, g_entropy = (t if t is None else t.to(torch.float32).contiguous()
@@ -341,7 +358,7 @@ class _Fused(torch.autograd.Function):
         dH, dW = _grads(c, H, W, None, W.dtype, False, need_dH, need_dW)
         _backward(c, lse, ent, g_logp, g_entropy, scale, dH, dW)
         ctx.kept = False
-        c.ws, c.head = None, None  # freed now; a second backward takes a new one
+        c.ws, c.head, c.keep = None, None, None  # freed now; a second backward takes a new one
         if torch.is_grad_enabled():
             dH, dW = (t if t is None else _Once.apply(t, H, W, g, g_ent) for t in (dH, dW))
         return dH, dW, None, None
