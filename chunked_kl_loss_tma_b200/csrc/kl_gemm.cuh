@@ -30,7 +30,8 @@
 //              per (row, tile) the sum of e = 2^(x - r) around the logit r of the
 //              row's own token and, when asked, the sum of e (x - r) for the
 //              entropy; optionally stores e.
-//   EPI_DLOGP  their backward with the row lse known: dS from the accumulator.
+//   EPI_DLOGP  their backward with the row lse known: dS from the accumulator, and
+//              per (row, 128 columns) the sum of p without the row's own token.
 //   DYN = 1    the token rows of the chunk are counted on the device (rows that
 //              take no part are left out before the contraction), so the number
 //              of tiles, the K extent and the K split come from *dyn.
@@ -115,6 +116,11 @@ enum { STORE_NONE = 0, STORE_SHIFTED = 1, STORE_EXP = 2 };
 struct ChunkPlan {
   int rows;
   int ksplit;
+};
+
+template <bool B>
+struct BoolConst {
+  static constexpr bool value = B;
 };
 
 struct GemmParams {
@@ -962,11 +968,15 @@ __global__ void __launch_bounds__((XF || EG == 2) ? kGemmThreadsXf : kGemmThread
           p.partials[static_cast<int64_t>(grow) * (p.tiles_n * EG) + tn * EG + group] =
               make_float4(shift, se, su, 0.f);
       } else if (EPI == EPI_DLOGP) {
-        // dS_j = -p_j (a + b (ln p_j + entropy)) + a [j = id], p_j = 2^(x - lse log2 e);
-        // rows past the chunk's last are written as 0 (dW contracts whole K blocks).
+        // dS_j = -p_j (a + b (ln p_j + entropy)) for the other tokens, p_j = 2^(x - lse
+        // log2 e), and their sum of p_j: the own token's entry is formed from it by
+        // logp_own_kernel, because 1 - p from its own p loses what the logit's and the
+        // lse's roundings are (1e-6) where p is near 1.  Rows past the chunk's last are
+        // written as 0 (dW contracts whole K blocks).
         const float s2 = rv ? p.rowin[grow].x : 0.f;
         const int id = rv ? p.ids[grow] : -1;
         const float4 rc = rv ? p.rowc[grow] : make_float4(0.f, 0.f, 0.f, 0.f);
+        float others = 0.f;
 #pragma unroll 1
         for (int c = cs; c < cs + kSlabs; ++c) {
           uint32_t v[32];
@@ -975,18 +985,30 @@ __global__ void __launch_bounds__((XF || EG == 2) ? kGemmThreadsXf : kGemmThread
           tmem_ld_wait();
           if (c == cs + kSlabs - 1) release(buf);
           const int cb = col0 + c * 32;
-          if (cb >= p.cols_valid) continue;
+          const int nvalid = p.cols_valid - cb, k = id - cb;
+          if (nvalid <= 0) continue;
+          float s4[4] = {0.f, 0.f, 0.f, 0.f};
+          auto slab = [&](auto edge) {  // edge: holds own tokens or ends the vocabulary
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float x = fmaf(__uint_as_float(v[i]), s2, -rc.w);
-            const float pr = ex2_approx(x);
-            float ds = -rc.x * pr;
-            if (rc.y != 0.f && pr > 0.f) ds = fmaf(-pr * rc.y, fmaf(x, kLn2f, rc.z), ds);
-            if (cb + i == id) ds += rc.x;
-            v[i] = __float_as_uint(rv ? ds : 0.f);
-          }
+            for (int i = 0; i < 32; ++i) {
+              const float x = fmaf(__uint_as_float(v[i]), s2, -rc.w);
+              const float pr = !edge.value || (i < nvalid && i != k) ? ex2_approx(x) : 0.f;
+              s4[i & 3] += pr;
+              float ds = -rc.x * pr;
+              if (rc.y != 0.f && pr > 0.f) ds = fmaf(-pr * rc.y, fmaf(x, kLn2f, rc.z), ds);
+              v[i] = __float_as_uint(rv ? ds : 0.f);
+            }
+          };
+          if (nvalid >= 32 && !__any_sync(0xffffffffu, static_cast<unsigned>(k) < 32u))
+            slab(BoolConst<false>{});
+          else
+            slab(BoolConst<true>{});
+          others += (s4[0] + s4[1]) + (s4[2] + s4[3]);
           store_box(v, 1.f, 0.f, cb, row0, false, false, warp_rows);
         }
+        if (rv)
+          reinterpret_cast<float*>(p.partials)[static_cast<int64_t>(grow) * (p.tiles_n * EG) +
+                                               tn * EG + group] = others;
       } else {
 #pragma unroll 1
         for (int c = cs; c < cs + kSlabs; ++c) {  // both halves: TMEM columns are contiguous

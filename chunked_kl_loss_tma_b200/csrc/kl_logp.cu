@@ -8,7 +8,8 @@
 //   logp_rows      lse, logp, ent; the policy loss's row loss and gradient; the rows'
 //                  gradient factors (e is dS up to one factor per row)
 //   logp_dlogits   only with an entropy term: e -> dS in place
-//                  (chunks that are recomputed: logp_coef, and gemm DLOGP gives dS)
+//                  (chunks that are recomputed: logp_coef, gemm DLOGP gives dS of the
+//                  other tokens and logp_own that of the rows' own)
 //   gemm ACCUM     dH parts = dS W, split over the vocabulary
 //   logp_dh        parts summed, scattered to their rows; the others zeroed
 //   gemm           dW (+)= dS^T H_c
@@ -268,6 +269,16 @@ int launch_dlogits(LCtx& c, int64_t k) {
                           c.at<float>(c.l.clogp), c.at<float4>(c.l.rowc));
 }
 
+// The own tokens' entries after gemm_rows<EPI_DLOGP>.
+int launch_own(LCtx& c, int64_t k) {
+  LaunchScope ls("logp_own", c.st, 0, c.in_chunk(k) * (4.0 * c.l.parts_v + 38));
+  return launch_dependent(logp_own_kernel, static_cast<unsigned>(cdiv(c.in_chunk(k), 8)), 256, c.st,
+                          c.at<__nv_bfloat16>(c.l.E), c.l.Vp, static_cast<int>(c.p->V),
+                          c.at<float>(c.l.part), c.l.parts_v, c.plan(k),
+                          static_cast<int>(c.in_chunk(k)), c.at<int>(c.l.cid),
+                          c.at<RowIn>(c.l.rowin), c.at<float4>(c.l.rowc));
+}
+
 int launch_mean(LCtx& c, const float* x, int64_t n, bool norm, float given, float* loss) {
   LaunchScope ls("logp_mean", c.st, 0, 4.0 * n);
   return launch_dependent(logp_mean_kernel, 1, 1024, c.st, x, n, norm ? &c.sc->norm : nullptr,
@@ -460,6 +471,7 @@ int kl_logp_bwd(const kl_logp_problem* p, void* ws, size_t ws_bytes, const float
                                 c.at<float>(c.l.factor)));
       }
       KL_TRY(gemm_rows<EPI_DLOGP>(c, k, true));
+      KL_TRY(launch_own(c, k));
     }
     KL_TRY(grads(c, k, dH, dW, accumulate_dW || k > 0));
   }

@@ -574,6 +574,37 @@ __global__ void logp_coef_kernel(const ChunkPlan* plan, int64_t c0, int in_chunk
   factor[i] = 1.f;
 }
 
+// The own tokens' entries of a recomputed chunk, one warp per compact row, from the sums
+// of the others' p (one per 128 columns, joined in a fixed order):
+//   dS_id = a (1 - p) - p b (ln p + ent),  1 - p = sum_{j != id} p_j,
+// where p near 1 comes from that sum too, and p elsewhere from the gathered logit.  For
+// log-probabilities of -1e-5 and nearer to 0, a - a p was wrong by all of its value.
+// 8192 rows, vocabulary 128256: 17 us beside the 6.8 ms of the chunk's logits (54 rows: 1.5
+// of 39.5 us of the call).
+__global__ void __launch_bounds__(256)
+    logp_own_kernel(__nv_bfloat16* E, int64_t ld, int V, const float* part, int parts_n,
+                    const ChunkPlan* plan, int in_chunk, const int* cid, const RowIn* rowin,
+                    const float4* rowc) {
+  grid_dep_wait();
+  const int lane = threadIdx.x & 31;
+  const int i = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (i >= rows_of(plan, in_chunk)) return;
+  const float* pr = part + static_cast<int64_t>(i) * parts_n;
+  float q = 0.f;
+#pragma unroll 8
+  for (int t = lane; t < parts_n; t += 32) q += pr[t];
+  q = warp_sum(q);
+  if (lane != 0) return;
+  const float4 rc = rowc[i];
+  const RowIn in = rowin[i];
+  const float l2 = in.ref - rc.w + in.ref_lo;
+  const float p = q < 0.5f ? 1.f - q : ex2_approx(l2);
+  const float lnp = q < 0.5f ? log1pf(-q) : l2 * kLn2;
+  const int id = min(max(cid[i], 0), V - 1);
+  E[static_cast<int64_t>(i) * ld + id] =
+      __float2bfloat16_rn(rc.x * q - p * rc.y * (lnp + rc.z));
+}
+
 // dS in place over the stored exponentials where the gradient has an entropy
 // term, one CTA per compact row (zeros up to the padded end):
 //   p_j = e_j 2^(shift - lse log2 e),  dS_j = -p_j (a + b (ln p_j + ent)),
