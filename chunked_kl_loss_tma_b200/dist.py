@@ -27,6 +27,10 @@ def shard_range(n_tokens: int, world: int, rank: int):
     return start, start + base + (1 if rank < extra else 0)
 
 
+def _world(group):
+    return dist.get_world_size(group) if dist.is_initialized() else 1
+
+
 def _nccl(group):
     return dist.is_initialized() and dist.get_backend(group) == "nccl"
 
@@ -104,7 +108,9 @@ def dp_kl_fwd_bwd(H, W, *, group=None, grad_loss=1.0, mask=None, reduce="all_red
     batch.  Returns dict(loss = the whole batch's loss, dH = this shard's rows,
     dW = the summed head gradient (reduce="all_reduce"), this rank's block of
     rows of it (reduce="reduce_scatter", rows dW_shard_rows(V, world, rank)) or
-    the local gradient (reduce="none"), n_valid = the global count, workspace)."""
+    the local gradient (reduce="none"), n_valid = the global count, workspace).
+    accumulate_dW adds this rank's share to dW before the exchange: dW has to hold this
+    rank's own sums then (of calls with reduce="none"), not the ranks'."""
     from . import ops
 
     if reduce not in ("all_reduce", "reduce_scatter", "none"):
@@ -132,6 +138,11 @@ def _combine(out, reduce, n_all, group):
 def _dp(fn, n_local, H, W, args, group, reduce, normalizer, kw):
     if reduce not in ("all_reduce", "reduce_scatter", "none"):
         raise ValueError(f"unknown reduce {reduce!r}")
+    if kw.get("accumulate_dW") and reduce != "none" and _world(group) > 1:
+        # the exchange would sum what dW held before over the ranks again
+        raise ValueError("accumulate_dW over several ranks needs reduce='none': add up every "
+                         "call's share, then exchange dW once (sum_over_ranks, "
+                         "reduce_scatter_rows)")
     n_all = global_valid_count(n_local, group) if dist.is_initialized() else n_local
     # a count of 0 over all ranks: no loss and no gradient, whatever the divisor
     out = fn(H, W, *args, normalizer=float(normalizer or n_all or 1), **kw)
@@ -143,7 +154,9 @@ def dp_policy_fwd_bwd(H, W, ids, advantage, *, group=None, mask=None, reduce="al
     """Policy loss, forward and backward, of this rank's token shard, combined over the
     ranks as dp_kl_fwd_bwd does.  normalizer: the whole batch's divisor; by default
     the number of rows that take part on all ranks.  reduce="all_reduce" sums dW in its
-    own type (pass dW_dtype float32, the default, for fp32 sums)."""
+    own type (pass dW_dtype float32, the default, for fp32 sums).  Several calls into one
+    dW: accumulate_dW with reduce="none", then sum_over_ranks(dW) or
+    reduce_scatter_rows(dW) once."""
     from . import logp
 
     keep = ids >= 0
