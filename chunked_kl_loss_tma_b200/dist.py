@@ -125,7 +125,9 @@ def dp_kl_fwd_bwd(H, W, *, group=None, grad_loss=1.0, mask=None, reduce="all_red
 def _combine(out, reduce, n_all, group):
     """The ranks' shares of loss and dW joined."""
     loss = out["loss"].reshape(1)
-    if reduce == "all_reduce":
+    if out["dW"] is None:  # need_dW=False
+        pass
+    elif reduce == "all_reduce":
         sum_over_ranks(out["dW"], group)
     elif reduce == "reduce_scatter":
         out["dW"] = reduce_scatter_rows(out["dW"], group)

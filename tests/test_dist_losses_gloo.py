@@ -73,6 +73,19 @@ def _accumulate(kd, rank, world):
     assert torch.allclose(dW, want)
 
 
+def _one_gradient(kd, rank, world):
+    """A frozen head: no dW to exchange."""
+    H, ids, adv = _batch(2)
+    W = _head()
+    a, b = kd.shard_range(N, world, rank)
+    whole = _whole(H, W, ids, adv)
+    for reduce in ("all_reduce", "reduce_scatter", "none"):
+        out = kd.dp_policy_fwd_bwd(H[a:b], W, ids[a:b], adv[a:b], reduce=reduce, need_dW=False)
+        assert out["dW"] is None
+        assert torch.allclose(out["loss"], whole["loss"])
+        assert torch.allclose(out["dH"], whole["dH"][a:b])
+
+
 def _worker(rank, world, port, what, q):
     from chunked_kl_loss_tma_b200 import dist as kd
     from chunked_kl_loss_tma_b200 import logp
@@ -89,8 +102,9 @@ def _worker(rank, world, port, what, q):
         dist.destroy_process_group()
 
 
-@pytest.mark.parametrize("what", ["_accumulate"])
-def test_ranks(what, world=2):
+@pytest.mark.parametrize("what,world", [("_accumulate", 2), ("_one_gradient", 1),
+                                        ("_one_gradient", 2)])
+def test_ranks(what, world):
     ctx = mp.get_context("spawn")
     q, port = ctx.Queue(), _free_port()
     procs = [ctx.Process(target=_worker, args=(r, world, port, what, q)) for r in range(world)]
