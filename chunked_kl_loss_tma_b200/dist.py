@@ -161,12 +161,15 @@ def dp_policy_fwd_bwd(H, W, ids, advantage, *, group=None, mask=None, reduce="al
     reduce_scatter_rows(dW) once."""
     from . import logp
 
-    keep = ids >= 0
+    # the rows that the device lets take part
+    N = ids.shape[0]
+    keep = (ids >= 0) & (ids < W.shape[0])
     if mask is not None:
         keep &= mask.bool()
     if cu_seqlens is not None:
-        row = torch.arange(ids.shape[0], device=ids.device)
-        keep &= (row >= cu_seqlens[0]) & (row < cu_seqlens[-1])
+        row = torch.arange(N, device=ids.device)
+        good = (cu_seqlens >= 0).all() & (cu_seqlens <= N).all() & (cu_seqlens.diff() >= 0).all()
+        keep &= (row >= cu_seqlens[0]) & (row < cu_seqlens[-1]) & good
     return _dp(logp.policy_fwd_bwd, int(keep.sum().item()), H, W, (ids, advantage), group, reduce,
                normalizer, dict(kw, mask=mask, cu_seqlens=cu_seqlens))
 

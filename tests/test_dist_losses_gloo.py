@@ -86,6 +86,28 @@ def _one_gradient(kd, rank, world):
         assert torch.allclose(out["dH"], whole["dH"][a:b])
 
 
+def _count(kd, rank, world):
+    """The rows that the device leaves out are not counted: tokens outside the vocabulary,
+    and every row of a rank whose offsets are bad."""
+    H, ids, adv = _batch(3)
+    W = _head()
+    ids = ids.clone()
+    ids[[1, 20]] = V
+    ids[[2, 21]] = V + 7
+    ids[5] = -100
+    whole = _whole(H, W, ids, adv)
+    a, b = kd.shard_range(N, world, rank)
+    out = kd.dp_policy_fwd_bwd(H[a:b], W, ids[a:b], adv[a:b])
+    assert out["n_valid"] == N - 5
+    assert torch.allclose(out["loss"], whole["loss"]) and torch.allclose(out["dW"], whole["dW"])
+    # offsets: good on rank 0 (rows 2 to 9), bad in one of three ways on rank 1
+    H, ids, adv = _batch(4)
+    for bad in ([0, 9, 4], [-1, 3, 9], [0, 9, 14]):
+        cu = torch.tensor([2, 5, 9] if rank == 0 else bad, dtype=torch.int32)
+        seen = kd.dp_policy_fwd_bwd(H[a:b], W, ids[a:b], adv[a:b], cu_seqlens=cu)["n_valid"]
+        assert seen == 7, (bad, seen)
+
+
 def _worker(rank, world, port, what, q):
     from chunked_kl_loss_tma_b200 import dist as kd
     from chunked_kl_loss_tma_b200 import logp
@@ -103,7 +125,7 @@ def _worker(rank, world, port, what, q):
 
 
 @pytest.mark.parametrize("what,world", [("_accumulate", 2), ("_one_gradient", 1),
-                                        ("_one_gradient", 2)])
+                                        ("_one_gradient", 2), ("_count", 2)])
 def test_ranks(what, world):
     ctx = mp.get_context("spawn")
     q, port = ctx.Queue(), _free_port()
