@@ -178,7 +178,8 @@ def dp_preference_fwd_bwd(H, W, ids, cu_seqlens, pairs=None, *, group=None, redu
                           normalizer=None, **kw):
     """Preference loss, forward and backward, of this rank's pairs (both sequences of a
     pair on one rank), combined over the ranks.  normalizer: by default the number of
-    pairs on all ranks (n_valid of the result)."""
+    pairs on all ranks (n_valid of the result).  A rank without pairs passes an empty
+    tensor [0, 2]."""
     from . import logp
 
     n = pairs.shape[0] if pairs is not None else (cu_seqlens.numel() - 1) // 2

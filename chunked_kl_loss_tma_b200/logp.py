@@ -249,7 +249,10 @@ def _preference(c, pairs, ref_logp=None, beta=0.1, loss="sigmoid", label_smoothi
         P = S // 2
     _need(ref_logp, "ref_logp", torch.float32, c.dev, shape=(S,))
     c.keep += (pairs, ref_logp)
-    return L.KLPreference(_ptr(pairs), P, _ptr(ref_logp), L.KL_PREFERENCE[loss],
+    at = _ptr(pairs)
+    if at == 0:  # no pairs: an address that is not read, since NULL asks for the default ones
+        at = c.p.cu_seqlens
+    return L.KLPreference(at, P, _ptr(ref_logp), L.KL_PREFERENCE[loss],
                           int(bool(average)), beta, label_smoothing, margin, normalizer)
 
 

@@ -418,7 +418,8 @@ int kl_policy_fwd_bwd(const kl_logp_problem* p, const kl_policy* q, void* ws, si
 #define KL_PREFERENCE_HINGE 2
 typedef struct kl_preference {
   const int32_t* pairs;    /* [n_pairs, 2] (chosen, rejected); NULL: (i, n_pairs + i),
-                              n_seqs = 2 n_pairs                                   */
+                              n_seqs = 2 n_pairs.  With n_pairs = 0 and sequences: any
+                              other address, which is not read                     */
   int64_t n_pairs;
   const float* ref_logp;   /* [n_seqs] reference scores, or NULL (0)              */
   int32_t loss;            /* KL_PREFERENCE_*                                     */
