@@ -69,6 +69,17 @@ def _table(src, dst=None):
     return table, len(src), dev
 
 
+_requires_grad = torch.Tensor.requires_grad.__get__
+
+
+def _no_parameters(ts):
+    """Refuses parameters, whose weights would be scaled (or overwritten) in place of
+    their gradients."""
+    if any(map(_requires_grad, ts)) and any(t.requires_grad and t.is_leaf for t in ts):
+        raise ValueError("a leaf that requires grad: pass its gradient (p.grad), not the "
+                         "parameter")
+
+
 def _norm_type(norm_type):
     if norm_type == 2:
         return L.KL_NORM_2
@@ -106,12 +117,16 @@ def grad_total(grads, *, norm_type=2.0):
 
 def clip_grad_norm_(grads, max_norm, *, norm_type=2.0, out=None, total=None):
     """Scales the gradients by min(1, max_norm / (norm + 1e-6)) and returns the norm
-    before (float32 device scalar).  In place, or into the tensors `out`, each rounded
-    once to its type.  In place nothing is written while the norm stays under
-    max_norm.  total: the float64 device scalar that grad_total gives (joined over
-    ranks, say) in place of the tensors' own.  A NaN norm gives NaN everywhere, an
+    before (float32 device scalar).  grads are the gradients themselves, not the
+    parameters: a leaf that requires grad is refused.  In place, or into the tensors
+    `out`, each rounded once to its type.  In place nothing is written while the norm
+    stays under max_norm.  total: the float64 device scalar that grad_total gives (joined
+    over ranks, say) in place of the tensors' own.  A NaN norm gives NaN everywhere, an
     infinite one zeros (NaN where a gradient is infinite)."""
+    grads, out = ([ts] if isinstance(ts, torch.Tensor) else ts if ts is None else list(ts)
+                  for ts in (grads, out))
     table, n, dev = _table(grads, out)
+    _no_parameters(grads if out is None else grads + out)
     kind, ws = _norm_type(norm_type), _scratch(n, dev)
     if total is not None and (not isinstance(total, torch.Tensor) or total.numel() != 1 or
                               total.dtype != torch.float64 or total.device != dev):
