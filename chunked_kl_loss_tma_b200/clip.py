@@ -12,12 +12,14 @@ import array
 import math
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import _lib as L
 from .ops import on_device
 
 _DT = {torch.bfloat16: L.KL_DTYPE_BF16, torch.float32: L.KL_DTYPE_F32,
        torch.float16: L.KL_DTYPE_F16}
+_PAIR = {t: k | k << 32 for t, k in _DT.items()}  # source and destination alike
 
 
 def _dense(t):
@@ -26,9 +28,17 @@ def _dense(t):
     return t.permute(order).is_contiguous()
 
 
-def _list(ts, name):
-    """The tensors as a list, their device, and the library's names of their types."""
-    ts = [ts] if isinstance(ts, torch.Tensor) else list(ts)
+def _gradient_dtype(t):
+    """t's type, where t requires grad: refuses parameters, whose weights would be scaled
+    (or overwritten) in place of their gradients."""
+    if t.is_leaf:
+        raise ValueError("a leaf that requires grad: pass its gradient (p.grad), not the "
+                         "parameter")
+    return t.dtype
+
+
+def _list(ts, name, kinds, clip):
+    """The tensors' device and what `kinds` names their types; clip: no parameters."""
     if not ts:
         raise ValueError(f"no {name}")
     try:
@@ -38,46 +48,43 @@ def _list(ts, name):
     if len(where) != 1 or where == {-1}:
         raise ValueError(f"{name} must be on one CUDA device")
     try:
-        return ts, ts[0].device, [_DT[t.dtype] for t in ts]
+        if not clip:
+            return ts[0].device, [kinds[t.dtype] for t in ts]
+        return ts[0].device, [kinds[_gradient_dtype(t) if t.requires_grad else t.dtype]
+                              for t in ts]
     except KeyError:
         raise TypeError(f"{name} must be float32, bfloat16 or float16") from None
 
 
-def _table(src, dst=None):
-    """The library's table of the tensors (an array that stays alive for the call),
-    their number and device."""
-    src, dev, st = _list(src, "gradients")
+def _table(src, dst=None, clip=False):
+    """The library's table of the tensors in the lists (an array that stays alive for the
+    call), their number and device."""
     if dst is None:
+        dev, kinds = _list(src, "gradients", _PAIR, clip)
         if not all(map(torch.Tensor.is_contiguous, src)) and not all(
                 t.is_contiguous() or _dense(t) for t in src):
             raise ValueError("a gradient with gaps or repeats in memory")
-        to = at = list(map(torch.Tensor.data_ptr, src))
-        dt = st
+        to = at = array.array("q", map(torch.Tensor.data_ptr, src))
     else:
-        dst, dev_d, dt = _list(dst, "destinations")
+        dev, st = _list(src, "gradients", _DT, clip)
+        dev_d, dt = _list(dst, "destinations", _DT, clip)
         if len(src) != len(dst) or dev_d != dev:
             raise ValueError(f"{len(src)} gradients on {dev}, {len(dst)} destinations on {dev_d}")
         for s, d in zip(src, dst):
             if s.shape != d.shape or not s.is_contiguous() or not d.is_contiguous():
                 raise ValueError("a destination must be contiguous, of its gradient's shape")
-        at, to = (list(map(torch.Tensor.data_ptr, ts)) for ts in (src, dst))
+        at, to = (array.array("q", map(torch.Tensor.data_ptr, ts)) for ts in (src, dst))
+        kinds = [a | b << 32 for a, b in zip(st, dt)]
     # kl_grad: src, dst, n, and the two 32-bit types in one word
-    kinds = [a | b << 32 for a, b in zip(st, dt)]
     table = array.array("q", bytes(32 * len(src)))
-    for column, values in enumerate((at, to, map(torch.Tensor.numel, src), kinds)):
-        table[column::4] = array.array("q", values)
+    table[::4], table[1::4] = at, to
+    table[2::4] = array.array("q", map(torch.Tensor.numel, src))
+    table[3::4] = array.array("q", kinds)
     return table, len(src), dev
 
 
-_requires_grad = torch.Tensor.requires_grad.__get__
-
-
-def _no_parameters(ts):
-    """Refuses parameters, whose weights would be scaled (or overwritten) in place of
-    their gradients."""
-    if any(map(_requires_grad, ts)) and any(t.requires_grad and t.is_leaf for t in ts):
-        raise ValueError("a leaf that requires grad: pass its gradient (p.grad), not the "
-                         "parameter")
+def _as_list(ts):
+    return [ts] if isinstance(ts, torch.Tensor) else list(ts)
 
 
 def _norm_type(norm_type):
@@ -93,7 +100,7 @@ def _scratch(n, dev):
 
 
 def _norm(grads, norm_type, dtype):
-    table, n, dev = _table(grads)
+    table, n, dev = _table(_as_list(grads))
     kind, ws = _norm_type(norm_type), _scratch(n, dev)
     out = torch.empty((), dtype=dtype, device=dev)
     total, norm = (out.data_ptr(), None) if dtype == torch.float64 else (None, out.data_ptr())
@@ -123,10 +130,8 @@ def clip_grad_norm_(grads, max_norm, *, norm_type=2.0, out=None, total=None):
     stays under max_norm.  total: the float64 device scalar that grad_total gives (joined
     over ranks, say) in place of the tensors' own.  A NaN norm gives NaN everywhere, an
     infinite one zeros (NaN where a gradient is infinite)."""
-    grads, out = ([ts] if isinstance(ts, torch.Tensor) else ts if ts is None else list(ts)
-                  for ts in (grads, out))
-    table, n, dev = _table(grads, out)
-    _no_parameters(grads if out is None else grads + out)
+    grads, out = _as_list(grads), None if out is None else _as_list(out)
+    table, n, dev = _table(grads, out, clip=True)
     kind, ws = _norm_type(norm_type), _scratch(n, dev)
     if total is not None and (not isinstance(total, torch.Tensor) or total.numel() != 1 or
                               total.dtype != torch.float64 or total.device != dev):
@@ -135,4 +140,5 @@ def clip_grad_norm_(grads, max_norm, *, norm_type=2.0, out=None, total=None):
     on_device(dev, "kl_grad_clip", table.buffer_info()[0], n, kind, float(max_norm),
               None if total is None else total.data_ptr(), ws.data_ptr(), ws.numel(),
               norm.data_ptr())
+    increment_version(grads if out is None else out)  # autograd refuses what was saved before
     return norm

@@ -17,6 +17,7 @@ bad offset shows in status(out["workspace"])."""
 from __future__ import annotations
 
 import torch
+from torch.autograd.graph import increment_version
 
 from . import _lib as L
 from .ops import _need, _ptr, _workspace, on_device
@@ -121,6 +122,7 @@ def _grads(c, H, W, dW, dW_dtype, accumulate, need_dH, need_dW):
         raise ValueError("a dW to write, but need_dW is False")
     else:
         _need(dW, "dW", dW_dtype, c.dev, shape=W.shape)
+        increment_version(dW)  # written through its address: autograd is told
     return torch.empty(H.shape, dtype=H.dtype, device=c.dev) if need_dH else None, dW
 
 

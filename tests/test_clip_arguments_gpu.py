@@ -1,5 +1,5 @@
 """clip_grad_norm_ writes through addresses: it refuses parameters, which its name may
-invite."""
+invite, and tells autograd which tensors it changed."""
 import pytest
 import torch
 
@@ -41,3 +41,47 @@ def test_gradients_of_a_step():
         for b, g in zip(before, grads):
             assert torch.allclose(g.detach(), b * (0.5 / (want + 1e-6)), rtol=1e-5, atol=0)
         assert norm.item() == pytest.approx(want, rel=1e-6)
+
+
+def test_autograd_sees_what_changed():
+    """A saved tensor that is clipped before its backward is an error there."""
+    for into in (False, True):
+        x = torch.ones(100, device="cuda", requires_grad=True)
+        y = x * 2  # saved by the square below
+        loss = y.square().sum()
+        if into:
+            ck.clip_grad_norm_([torch.ones(100, device="cuda")], 0.1, out=[y.detach()])
+        else:
+            ck.clip_grad_norm_([y.detach()], 0.1)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+    src = torch.ones(100, device="cuda")
+    at = src._version
+    ck.clip_grad_norm_([src], 0.1, out=[torch.empty_like(src)])
+    ck.grad_norm([src])
+    assert src._version == at  # only read
+
+
+def test_inference_tensors():
+    """They have no version to count, and are clipped as before."""
+    with torch.inference_mode():
+        a = torch.full((100,), 2.0, device="cuda")
+    norm = ck.clip_grad_norm_([a], 1.0)
+    assert norm.item() == 20 and a[0].item() == pytest.approx(2 / 20, rel=1e-6)
+
+
+def test_autograd_sees_an_accumulated_head_gradient():
+    """The dW that a loss writes, likewise."""
+    g = torch.Generator().manual_seed(0)
+    H = torch.randn(20, 64, generator=g).bfloat16().cuda()
+    W = torch.randn(100, 64, generator=g).bfloat16().cuda()
+    ids, one = torch.arange(20, device="cuda"), torch.ones(20, device="cuda")
+    cu = torch.tensor([0, 8, 20], dtype=torch.int32, device="cuda")
+    dW = torch.zeros(100, 64, device="cuda")
+    lse = ck.logp_fwd(H, W, ids)["lse"]
+    for call in (lambda: ck.policy_fwd_bwd(H, W, ids, one, dW=dW, accumulate_dW=True),
+                 lambda: ck.preference_fwd_bwd(H, W, ids, cu, dW=dW, accumulate_dW=True),
+                 lambda: ck.logp_bwd(H, W, ids, lse, one, dW=dW)):
+        at = dW._version
+        call()
+        assert dW._version > at
