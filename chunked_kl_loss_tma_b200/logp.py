@@ -27,6 +27,16 @@ def _rows(t, name, dev, n):
     return _need(t, name, torch.float32, dev, shape=(n,))
 
 
+def _row_distance(H):
+    """Values from one row of H to the next, 0 where it is contiguous."""
+    if H.is_contiguous():
+        return 0
+    ldH = H.stride(0)  # rows at a distance: a slice of a wider tensor, say
+    if H.stride(1) != 1 or ldH < H.shape[1] or ldH % 8:
+        raise ValueError("the rows of H must be contiguous, a multiple of 8 values apart")
+    return ldH
+
+
 def make_logp_problem(H, W, ids, *, T=1.0, mask=None, chunk_tokens=0, want_entropy=False,
                       keep_chunk=False, cu_seqlens=None, dW_dtype=torch.float32):
     """Fill a kl_logp_problem from tensors.  Returns (problem, tensors kept alive)."""
@@ -38,11 +48,7 @@ def make_logp_problem(H, W, ids, *, T=1.0, mask=None, chunk_tokens=0, want_entro
     _need(W, "W", H.dtype, dev)
     if H.dim() != 2 or W.dim() != 2 or H.shape[1] != W.shape[1]:
         raise ValueError("H must be [N, d] and W [V, d]")
-    ldH = 0
-    if not H.is_contiguous():  # rows at a distance: a slice of a wider tensor, say
-        ldH = H.stride(0)
-        if H.stride(1) != 1 or ldH < H.shape[1] or ldH % 8:
-            raise ValueError("the rows of H must be contiguous, a multiple of 8 values apart")
+    ldH = _row_distance(H)
     N = H.shape[0]
     _need(ids, "ids", None, dev, shape=(N,))
     if ids.dtype not in (torch.int32, torch.int64):
@@ -88,14 +94,11 @@ class _Call:
         """The same problem with its tensors where they are now: saved tensors may have come
         back at other addresses (a head that was freed and gathered again, hooks that keep
         them on the host)."""
-        old = self.p
-        p, self.keep = make_logp_problem(
-            H, W, ids, T=old.T if T_row is None else T_row, mask=mask, cu_seqlens=cu_seqlens,
-            chunk_tokens=old.chunk_tokens, want_entropy=old.entropy, keep_chunk=old.keep_chunk,
-            dW_dtype=W.dtype)
-        if H.device != self.dev or (p.N, p.d, p.V, p.n_seqs) != (old.N, old.d, old.V, old.n_seqs):
-            raise ValueError("saved tensors of another shape or device than the forward's")
-        self.p = p
+        p = self.p
+        p.ldH = _row_distance(H)
+        p.H, p.W, p.ids, p.mask, p.T_row, p.cu_seqlens = map(
+            _ptr, (H, W, ids, mask, T_row, cu_seqlens))
+        self.keep = H, W, ids, mask, T_row, cu_seqlens
 
     def new(self, *shape):
         return torch.empty(shape, dtype=torch.float32, device=self.dev)
@@ -315,6 +318,22 @@ class _Once(torch.autograd.Function):
         raise RuntimeError("the fused losses have no second derivatives")
 
 
+def _kinds(ts):
+    return [None if t is None else (t.shape, t.get_device(), t.dtype) for t in ts]
+
+
+def _check_saved(ts, kinds):
+    """Saved tensors are what they were, wherever they are now (hooks may have moved them)."""
+    if _kinds(ts) != kinds:
+        for t, k in zip(ts, kinds):
+            if t is not None and t.dtype != k[2]:
+                raise TypeError(f"a saved tensor came back as {t.dtype}, not {k[2]}")
+        raise ValueError("a saved tensor came back with another shape or on another device")
+    for t in ts[1:]:  # rows of H may lie apart
+        if t is not None and not t.is_contiguous():
+            raise ValueError("a saved tensor came back with gaps")
+
+
 class _Fused(torch.autograd.Function):
     """Forward run(call) with the row gradients of a scalar loss (or, without "loss",
     logp and entropy themselves); backward kl_logp_bwd, from the kept chunk the first
@@ -331,8 +350,10 @@ class _Fused(torch.autograd.Function):
         ctx.scalar = "loss" in f
         ctx.set_materialize_grads(False)  # an entropy that no loss uses costs no pass
         # ids, mask, T and cu_seqlens too: the backward reads them again
-        ctx.save_for_backward(H, W, f["lse"], f.get("entropy"), f.get("g_logp"),
-                              f.get("g_entropy"), *call.keep[2:6])
+        saved = (H, W, f["lse"], f.get("entropy"), f.get("g_logp"), f.get("g_entropy"),
+                 *call.keep[2:6])
+        ctx.save_for_backward(*saved)
+        ctx.kinds = _kinds(saved)
         call.keep = None  # from here on autograd's saved tensors are what is held and read
         if ctx.scalar:
             return f["loss"]
@@ -341,11 +362,11 @@ class _Fused(torch.autograd.Function):
     @staticmethod
     def backward(ctx, g, g_ent=None):
         # refuses inputs that changed in place since the forward
-        H, W, lse, ent, g_logp, g_entropy, *rest = ctx.saved_tensors
+        saved = ctx.saved_tensors
+        _check_saved(saved, ctx.kinds)
+        H, W, lse, ent, g_logp, g_entropy, *rest = saved
         c, scale = ctx.call, g
         c.rebind(H, W, *rest)
-        for t in (lse, ent, g_logp, g_entropy):
-            _rows(t, "a saved tensor", c.dev, c.N)
         if not ctx.scalar:
             scale = None
             g_logp, g_entropy = (t if t is None else t.to(torch.float32).contiguous()
