@@ -355,6 +355,8 @@ class _Fused(torch.autograd.Function):
         ctx.save_for_backward(*saved)
         ctx.kinds = _kinds(saved)
         call.keep = None  # from here on autograd's saved tensors are what is held and read
+        if not ctx.kept:
+            call.ws = call.head = None
         if ctx.scalar:
             return f["loss"]
         return (f["logp"], f["entropy"]) if f["entropy"] is not None else f["logp"]
@@ -400,8 +402,10 @@ def _fused(run, H, W, ids, keep_chunk, **kw):
 def fused_logp(H, W, ids, *, want_entropy=False, keep_chunk=True, T=1.0, mask=None,
                chunk_tokens=0, cu_seqlens=None):
     """Differentiable log-probabilities [N] (with want_entropy: and entropies [N]) with
-    respect to H and W.  keep_chunk: the first chunk's logits stay allocated until the
-    backward, which then recomputes the other chunks only."""
+    respect to H and W.  keep_chunk: the workspace of both passes
+    (kl_logp_workspace_bytes, KL_ENTRY_FWD_BWD) stays allocated until the backward, which
+    takes the first chunk's logits from it and recomputes the other chunks only.  False:
+    nothing stays but a few numbers per row, and every chunk is recomputed."""
     _, apply = _fused(_logp, H, W, ids, keep_chunk, want_entropy=want_entropy, T=T, mask=mask,
                       chunk_tokens=chunk_tokens, cu_seqlens=cu_seqlens)
     return apply()

@@ -121,3 +121,26 @@ def test_checkpointed():
         loss = checkpoint(body, h, use_reentrant=False) if wrap else body(h)
         out.append((loss.detach(), *torch.autograd.grad(loss, (h, w))))
     assert all(torch.equal(a, b) for a, b in zip(*out))
+
+
+def test_without_a_kept_chunk_nothing_is_held():
+    """keep_chunk=False: a few numbers per row stay allocated between the passes, not the
+    forward's workspace; and inputs that only the forward reads are let go."""
+    H, W, ids = _inputs(4)
+    W.requires_grad_()
+    adv, mb = torch.ones(N, device="cuda"), 1 << 20
+    ck.fused_policy_loss(H, W, ids, adv, keep_chunk=False)
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    big = torch.zeros(1 << 22, device="cuda")
+    weight = big[:N]
+    loss = ck.fused_policy_loss(H, W, ids, adv, row_weight=weight, keep_chunk=False)
+    del big, weight
+    held = torch.cuda.memory_allocated() - before
+    assert held < 32 * N + 8192, held
+    kept = ck.fused_policy_loss(H, W, ids, adv)
+    assert torch.cuda.memory_allocated() - before > mb  # the kept chunk, until its backward
+    (loss + kept).backward()
+    del loss, kept
+    W.grad = None
+    assert torch.cuda.memory_allocated() - before < 8192
