@@ -392,7 +392,17 @@ class _Fused(torch.autograd.Function):
         return dH, dW, None, None
 
 
+def _constants(**rows):
+    """Refuses row inputs that require grad: the losses differentiate H and W alone."""
+    if torch.is_grad_enabled():
+        for name, t in rows.items():
+            if isinstance(t, torch.Tensor) and t.requires_grad:
+                raise ValueError(f"{name} requires grad, but gradients reach H and W alone: pass "
+                                 f"{name}.detach()")
+
+
 def _fused(run, H, W, ids, keep_chunk, **kw):
+    _constants(T=kw["T"])
     keep = keep_chunk and torch.is_grad_enabled() and (H.requires_grad or W.requires_grad)
     entry = L.KL_ENTRY_FWD_BWD if keep else L.KL_ENTRY_FWD
     c = _Call(entry, None, H.detach(), W.detach(), ids, keep_chunk=keep, dW_dtype=W.dtype, **kw)
@@ -405,7 +415,8 @@ def fused_logp(H, W, ids, *, want_entropy=False, keep_chunk=True, T=1.0, mask=No
     respect to H and W.  keep_chunk: the workspace of both passes
     (kl_logp_workspace_bytes, KL_ENTRY_FWD_BWD) stays allocated until the backward, which
     takes the first chunk's logits from it and recomputes the other chunks only.  False:
-    nothing stays but a few numbers per row, and every chunk is recomputed."""
+    nothing stays but a few numbers per row, and every chunk is recomputed.  A T that
+    requires grad is refused."""
     _, apply = _fused(_logp, H, W, ids, keep_chunk, want_entropy=want_entropy, T=T, mask=mask,
                       chunk_tokens=chunk_tokens, cu_seqlens=cu_seqlens)
     return apply()
@@ -415,7 +426,9 @@ def fused_policy_loss(H, W, ids, advantage, *, old_logp=None, ref_logp=None, row
                       clip_low=0.2, clip_high=0.2, dual_clip=0.0, kl_coef=0.0, entropy_coef=0.0,
                       normalizer=0.0, keep_chunk=True, T=1.0, mask=None, chunk_tokens=0,
                       cu_seqlens=None):
-    """Differentiable clipped policy loss (options as policy_fwd)."""
+    """Differentiable clipped policy loss (options as policy_fwd; keep_chunk as fused_logp).
+    Row inputs that require grad are refused."""
+    _constants(advantage=advantage, old_logp=old_logp, ref_logp=ref_logp, row_weight=row_weight)
     c, apply = _fused(lambda c: _policy_fwd(c, q), H, W, ids, keep_chunk,
                       want_entropy=entropy_coef != 0, T=T, mask=mask, chunk_tokens=chunk_tokens,
                       cu_seqlens=cu_seqlens)
@@ -426,9 +439,11 @@ def fused_policy_loss(H, W, ids, advantage, *, old_logp=None, ref_logp=None, row
 
 def fused_preference_loss(H, W, ids, cu_seqlens, pairs=None, *, keep_chunk=True, T=1.0,
                           mask=None, chunk_tokens=0, **options):
-    """Differentiable preference loss (options as preference_fwd)."""
+    """Differentiable preference loss (options as preference_fwd; keep_chunk as fused_logp).
+    Reference scores that require grad are refused."""
     if cu_seqlens is None:
         raise ValueError("cu_seqlens is required")
+    _constants(ref_logp=options.get("ref_logp"))
     c, apply = _fused(lambda c: _preference_fwd(c, q), H, W, ids, keep_chunk, T=T, mask=mask,
                       chunk_tokens=chunk_tokens, cu_seqlens=cu_seqlens)
     q = _preference(c, pairs, **options)

@@ -144,3 +144,29 @@ def test_without_a_kept_chunk_nothing_is_held():
     del loss, kept
     W.grad = None
     assert torch.cuda.memory_allocated() - before < 8192
+
+
+def test_row_inputs_that_require_grad_are_refused():
+    """They are constants of the losses: no gradient would reach them."""
+    H, W, ids = _inputs(5)
+    W.requires_grad_()
+    cu = torch.tensor([0, 100, 300], dtype=torch.int32, device="cuda")
+    one, two = torch.ones(N, device="cuda"), torch.ones(2, device="cuda")
+    leaf, leaf2 = one.clone().requires_grad_(), two.clone().requires_grad_()
+    calls = [
+        lambda x, y: ck.fused_logp(H, W, ids, T=x),
+        lambda x, y: ck.fused_policy_loss(H, W, ids, x),
+        lambda x, y: ck.fused_policy_loss(H, W, ids, one, old_logp=x),
+        lambda x, y: ck.fused_policy_loss(H, W, ids, one, ref_logp=x, kl_coef=0.1),
+        lambda x, y: ck.fused_policy_loss(H, W, ids, one, row_weight=x),
+        lambda x, y: ck.fused_policy_loss(H, W, ids, one, T=x),
+        lambda x, y: ck.fused_preference_loss(H, W, ids, cu, ref_logp=y),
+        lambda x, y: ck.fused_preference_loss(H, W, ids, cu, T=x),
+    ]
+    for k, call in enumerate(calls):
+        with pytest.raises(ValueError, match="require"):
+            call(leaf, leaf2)
+            pytest.fail(f"call {k} was not refused")
+        call(leaf.detach(), leaf2.detach()).sum().backward()
+        with torch.no_grad():
+            call(leaf, leaf2)
