@@ -204,13 +204,18 @@ __global__ void __launch_bounds__(1024)
   number_rows<1024>(sel, T_row, o, true, -1, nullptr);
 }
 
-// The tensor core adds each K = 16 step into the fp32 accumulator and truncates
-// towards zero.  A truncation loses on average a fixed share of the accumulator,
-// which grows on average in proportion to the steps done, so the finished logit
-// is short by a factor 1 - c steps.  Measured slope of (logit - exact logit) on
-// the exact logit, d = 512 to 8192: -1.6e-8 per step (-4.1e-6 at d = 4096).  The
-// logits' scale carries the inverse; the log-probabilities' relative error
-// falls from 2.3e-5 to 2.7e-6 at d = 4096 and a mean log-probability of -0.8.
+// The tensor core adds each K = 16 step into the fp32 accumulator and truncates towards
+// zero, which takes a share of what the accumulator holds at each step.  Over a logit
+// whose products add up in one direction that is between nothing (all of it in one step,
+// the others add 0) and twice c steps (all of it in the first step, small products in the
+// others); c steps where it grows evenly, as with products that are alike along d.
+// Measured slope of (logit - exact logit) on the exact logit there, d = 512 to 8192:
+// -1.6e-8 per step (-4.1e-6 at d = 4096).  The logits' scale carries the inverse, the
+// middle of the two.  The own token's logit is formed apart and needs none.  Rms errors
+// of log-probabilities at d = 4096, without and with it: even growth 5.8e-7 and 3.4e-8
+// (tokens at -0.12), 3.9e-6 and 4.0e-7 (at -9.5); cancelling halves 4.2e-7 and 5.2e-7;
+// all of the logit in one step 2.7e-7 and 2.6e-5 (logits up to 32): within the bound
+// that any input has, 2^-23 per step of the largest partial sum.
 constexpr double kTruncPerStep = 1.62e-8;
 
 // What the logits epilogue and the row kernels know of a compact row beforehand.
