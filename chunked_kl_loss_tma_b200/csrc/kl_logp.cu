@@ -22,6 +22,11 @@ using namespace ckl;
 
 namespace {
 
+// Rows per chunk by default.  In one pass 4096 are as fast (policy loss, 8192 to 32768
+// rows, bf16 dW: d 4096, V 128256 20.3, 40.9 and 81.4 ms with 8192, 20.0, 39.9 and 79.1
+// with 4096; d 2048, V 50257 3.9, 8.2 and 16.2 against 4.0, 8.1 and 16.0) in half the
+// workspace; but where the backward follows a forward over all rows only the first
+// chunk's logits are kept, and a row behind it costs a third more.
 constexpr int64_t kLogpChunk = 8192;
 constexpr int kMaxSeqs = 1 << 20;
 

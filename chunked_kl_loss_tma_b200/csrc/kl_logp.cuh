@@ -15,7 +15,7 @@
 // consecutively (compact rows), their hidden states are gathered, and the
 // contractions run over them alone, with the counts read on the device.  In a
 // policy step with 35% of the rows masked that is a third of the work; the
-// gather costs 6 d bytes a row (17 us for 2663 of 4096 rows at d 4096, of 5.5 ms).
+// gather costs 6 d bytes a row (17 us for 2663 of 4096 rows at d 4096, of 6.7 ms).
 #pragma once
 #include <cuda_bf16.h>
 #include <math.h>
@@ -376,9 +376,10 @@ struct RowOut {
 // stored exponentials are dS up to one factor per row.  So no pass over the chunk
 // turns them into dS.  The own token's entry becomes e_id - Z = -(sum of the
 // others), accurate however near 1 its probability is; the factor goes onto the
-// rows of dH as they are summed, and onto the rows of H that dW contracts (one
-// rounding to bf16, in place of that of dS).  At 8192 rows and a vocabulary of
-// 128256 the pass took 0.75 of 19.5 ms.  With an entropy term (b != 0) the
+// rows of dH as they are summed, and onto the rows of H that dW contracts.  So dW's
+// products carry two roundings to bf16, of e and of the scaled row, where a stored dS
+// has one: 2.3e-3 from the 64-bit dW, in fp32 or bf16, where one rounding of the result
+// is 1.7e-3.  At 8192 rows and a vocabulary of 128256 the pass took 0.75 of 19.5 ms.  With an entropy term (b != 0) the
 // factor differs along the row and the pass runs (logp_dlogits_kernel).
 struct RowBack {
   __nv_bfloat16* E;     // stored exponentials [.][ld], or nullptr: no gradient wanted

@@ -322,7 +322,8 @@ typedef struct kl_logp_problem {
   int64_t V;               /* vocabulary size (rows of W)                         */
   int32_t dtype;           /* KL_DTYPE_BF16: H, W and dH                          */
   int32_t dW_dtype;        /* KL_DTYPE_F32 or KL_DTYPE_BF16: type of dW.  bf16 is
-                              rounded once, from fp32 sums over all chunks         */
+                              rounded once, from fp32 sums over all chunks; in both
+                              the operands (exponentials, rows of H) are bf16       */
   const void* H;           /* [N, d], rows ldH apart                              */
   const void* W;           /* [V, d]                                              */
   const void* ids;         /* [N] token of each row; negative: takes no part       */
@@ -473,7 +474,9 @@ int kl_grad_clip(const kl_grad* g, int64_t count, int norm_type, float max_norm,
 
 /* Synchronises stream, then returns the device-side status recorded in ws
  * (KL_OK, KL_ERR_INDEX or KL_ERR_TIMEOUT), or KL_ERR_CUDA if the stream
- * reports an error.  Does not clear it; every kl_* call resets it at start. */
+ * reports an error.  Does not clear it; every kl_* call resets it at start, but
+ * for a kl_logp_bwd with keep_chunk, which belongs to the forward before it, and the
+ * kl_grad_* calls, whose workspace has none. */
 int kl_status(void* ws, void* stream);
 
 /* Static English description of a status code. */
