@@ -146,6 +146,30 @@ def test_without_a_kept_chunk_nothing_is_held():
     assert torch.cuda.memory_allocated() - before < 8192
 
 
+def test_hooks_free_the_originals():
+    """Saved tensors that hooks move to the host are not held on the device as well."""
+    n = 4096
+    g = torch.Generator().manual_seed(6)
+    base = torch.randn(n, D, generator=g).bfloat16().cuda().requires_grad_()
+    W = torch.randn(V, D, generator=g).bfloat16().cuda().requires_grad_()
+    ids, adv = torch.randint(V, (n,), generator=g).cuda(), torch.ones(n, device="cuda")
+    grads = []
+    for hooks in (False, True):
+        before = torch.cuda.memory_allocated()
+        h = base * 2
+        if hooks:
+            with torch.autograd.graph.save_on_cpu():
+                loss = ck.fused_policy_loss(h, W, ids, adv, keep_chunk=False)
+        else:
+            loss = ck.fused_policy_loss(h, W, ids, adv, keep_chunk=False)
+        del h
+        held = torch.cuda.memory_allocated() - before
+        assert held < 8192 if hooks else held >= base.numel() * 2, held
+        grads.append(torch.autograd.grad(loss, (base, W)))
+        del loss
+    assert all(torch.equal(a, b) for a, b in zip(*grads))
+
+
 def test_row_inputs_that_require_grad_are_refused():
     """They are constants of the losses: no gradient would reach them."""
     H, W, ids = _inputs(5)
