@@ -379,8 +379,9 @@ struct RowOut {
 // rows of dH as they are summed, and onto the rows of H that dW contracts.  So dW's
 // products carry two roundings to bf16, of e and of the scaled row, where a stored dS
 // has one: 2.3e-3 from the 64-bit dW, in fp32 or bf16, where one rounding of the result
-// is 1.7e-3.  At 8192 rows and a vocabulary of 128256 the pass took 0.75 of 19.5 ms.  With an entropy term (b != 0) the
-// factor differs along the row and the pass runs (logp_dlogits_kernel).
+// is 1.7e-3.  At 8192 rows and a vocabulary of 128256 the pass took 0.75 of 19.5 ms.
+// With an entropy term (b != 0) the factor differs along the row and the pass runs
+// (logp_dlogits_kernel).
 struct RowBack {
   __nv_bfloat16* E;     // stored exponentials [.][ld], or nullptr: no gradient wanted
   int64_t ld;

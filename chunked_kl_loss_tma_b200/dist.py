@@ -191,8 +191,8 @@ def dp_clip_grad_norm_(grads, max_norm, *, sharded=(), group=None, norm_type=2.0
     """clip_grad_norm_ where the ranks hold different parts of some gradients: `sharded`
     lists this rank's parts (its rows of a reduce-scattered dW, say), `grads` the
     tensors that are the same on every rank.  A rank that holds no part passes an empty
-    tensor.  One all-reduce of 8 bytes; no synchronisation with NCCL.  out: destinations for grads, then for sharded.
-    Returns the norm over all ranks."""
+    tensor.  One all-reduce of 8 bytes; no synchronisation with NCCL.  out: destinations
+    for grads, then for sharded.  Returns the norm over all ranks."""
     from . import clip
 
     grads = [grads] if isinstance(grads, torch.Tensor) else list(grads)

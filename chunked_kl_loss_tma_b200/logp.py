@@ -12,8 +12,9 @@ include/chunked_kl.h for what each computes and which rows take part).
 H [N, d] (its rows may lie apart, as in a slice) and W [V, d] are bfloat16.  ids [N]
 are int32 or int64.  A row takes no part when mask is 0 there, its id is negative
 (-1, -100) or it lies outside the packed sequences of cu_seqlens; its outputs and
-gradients are 0 and it costs no work.  Everything is enqueued on the current stream of H's device; an id >= V or a
-bad offset shows in status(out["workspace"])."""
+gradients are 0 and it costs no work.  A NaN in a row that takes part reaches the loss
+and the gradients.  Everything is enqueued on the current stream of H's device; an id >= V
+or a bad offset shows in status(out["workspace"])."""
 from __future__ import annotations
 
 import torch
